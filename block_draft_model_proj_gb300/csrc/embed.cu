@@ -127,19 +127,25 @@ embed_kernel(const T* __restrict__ table, int V, int D, const int32_t* __restric
         for (int h = 0; h < kHold; ++h)
           if (c0 + h * tx < nvec)
             load_pack<T, kN>(table + (size_t)id[q] * D + (size_t)(c0 + h * tx) * kN, v[q][h]);
+      } else if (q == 0) {
+        // the row of the batch before goes on: out of the last slot's registers before that
+        // slot's own load (scaled already)
+#pragma unroll
+        for (int h = 0; h < kHold; ++h)
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[0][h][e] = v[kBatch - 1][h][e];
       }
     }
     const int was = last;
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      const int before = q ? id[q - 1] : was;
+      const bool same = id[q] == (q ? id[q - 1] : was);
       if (id[q] == -2) break;
 #pragma unroll
       for (int h = 0; h < kHold; ++h) {
 #pragma unroll
         for (int e = 0; e < kN; ++e)
-          v[q][h][e] = id[q] < 0 ? 0.f
-                       : id[q] == before ? v[q ? q - 1 : kBatch - 1][h][e] : v[q][h][e] * scale;
+          v[q][h][e] = id[q] < 0 ? 0.f : same ? v[q ? q - 1 : 0][h][e] : v[q][h][e] * scale;
         if (c0 + h * tx < nvec)
           store_pack<T, kN>(out + (size_t)(t0 + r0 + q) * D + (size_t)(c0 + h * tx) * kN, v[q][h]);
       }

@@ -281,3 +281,37 @@ def test_given_streams(lib):
         junk = torch.full((1 << 20,), 7.0, device="cuda")   # would take a freed workspace's place
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(e, emb) and junk.eq(7).all()
+
+
+def _walk_ids(rng, T, V, kind):
+    """Tokens whose changes fall on every place of a walk over consecutive slots."""
+    if kind == "few":           # two or three tokens in all: repeats and changes anywhere
+        return rng.integers(0, min(V, 3), T).astype(np.int32)
+    if kind == "text":          # plain text: a frequent token among others
+        return np.where(rng.random(T) < 0.5, 7 % V, rng.integers(0, V, T)).astype(np.int32)
+    ids = np.where(np.arange(T) % kind == 0, rng.integers(0, V, T), V - 1)
+    ids[rng.random(T) < 0.05] = -1      # single empty slots
+    return ids.astype(np.int32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", [3, 5, 6, 7, 10, 16, "few", "text"])
+@pytest.mark.parametrize("T,V,D", [(2600, 300, 4096), (8195, 900, 4096), (2600, 300, 1001),
+                                   (1003, 40, 2050), (20011, 500, 520)])
+def test_forward_of_long_walks(lib, T, V, D, kind, dtype):
+    """Enough slots that a row of threads takes many consecutive ones (up to 16), whose rows
+    stay in its registers while the token repeats."""
+    import torch
+    import block_draft_model_proj_gb300 as dflash
+    rng = np.random.default_rng(T + D)
+    table = torch.as_tensor(rng.standard_normal((V, D)).astype(np.float32)).cuda().to(_dt(dtype))
+    ids = torch.as_tensor(_walk_ids(rng, T, V, kind)).cuda()
+    rows = table.double()[ids.long().clamp(min=0)] * (ids >= 0)[:, None]
+    for scale in (1.0, 1.7):
+        buf, out = _guarded((T, D), table.dtype)
+        dflash.dflash_embed_tokens(table, ids, out, scale=scale)
+        dflash.dflash_device_status()
+        assert _guards_ok(buf)
+        wrong = (out.double() - scale * rows).abs() > \
+            (0.0 if scale == 1.0 else _half(dtype) + 2 * 2.0 ** -24) * (scale * rows).abs()
+        assert not wrong.any(), wrong.any(1).nonzero()[:8, 0].tolist()
