@@ -955,16 +955,18 @@ __global__ void __launch_bounds__(kNT, 1024 / kNT) filter_kernel(const FilterArg
     }
     spread = true;
   }
-  if (spread && pivot > kLowest && pivot < INFINITY) {
+  if (spread && pivot < INFINITY) {  // a pivot of kLowest too: it can hold the cut by index
     const int b = __float_as_int(pivot);
     above_pivot = pivot == 0.f ? __int_as_float(1) : __int_as_float(pivot > 0.f ? b + 1 : b - 1);
   }
+  // some token above -inf is not kept
+  const bool partial = pivot > kLowest || cut != 0x7fffffff;
   if (spread && by_value) {
     if constexpr (!kVerify) {
       // fast sums first where the smallest kept weight is well above their error
       u64 about;
       if (fast_ok && units(pivot) > z >> (kFastBits - 3))
-        token = search_fast<T, kNT>(cl, sh, sl, rank, C, pivot > kLowest, kept,
+        token = search_fast<T, kNT>(cl, sh, sl, rank, C, partial, kept,
                                     least_kept, FastScale(mx, chi, clo), units, u, &about);
       if (token < 0) token = value_search();
     }
@@ -981,7 +983,7 @@ __global__ void __launch_bounds__(kNT, 1024 / kNT) filter_kernel(const FilterArg
       z = cluster_sum(s);
     } else {
       if (fast_ok)
-        token = search_fast<T, kNT>(cl, sh, sl, rank, C, pivot > kLowest, kept,
+        token = search_fast<T, kNT>(cl, sh, sl, rank, C, partial, kept,
                                     least_kept, FastScale(mx, chi, clo), units, u, &z);
       if (token < 0)
         token = search<T, kNT>(cl, sh, sl, rank, C, w_kept,
