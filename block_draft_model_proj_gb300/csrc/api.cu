@@ -4,6 +4,7 @@
 #include <stdarg.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 #include <stdio.h>
@@ -272,6 +273,18 @@ int check_ws(void* ws, size_t ws_bytes, size_t need) {
 int check_elem_aligned(const void* p, const char* what, int dtype) {
   if ((uintptr_t)p % (dtype == DFLASH_DTYPE_F32 ? 4 : 2) != 0)
     return fail(DFLASH_ERR_INVALID_ARG, "%s must be aligned to its element size", what);
+  return DFLASH_OK;
+}
+
+// ... and so do arrays of 32-bit values (optional ones may be null).
+struct Named {
+  const void* p;
+  const char* what;
+};
+int check_words(std::initializer_list<Named> list) {
+  for (const Named& n : list)
+    if ((uintptr_t)n.p % 4 != 0)
+      return fail(DFLASH_ERR_INVALID_ARG, "%s must be aligned to its element size", n.what);
   return DFLASH_OK;
 }
 
@@ -1140,6 +1153,7 @@ int dflash_embed_tokens(const void* table, int dtype, int V, int D, const int32_
   if ((r = check_embed(dtype, V, D, T, scale))) return r;
   if (T == 0) return DFLASH_OK;
   if (!token_ids) return fail(DFLASH_ERR_INVALID_ARG, "token_ids is null");
+  if ((r = check_words({{token_ids, "token_ids"}}))) return r;
   if ((r = check_ptr16(table, "table", dtype))) return r;
   if ((r = check_ptr16(out, "out", dtype))) return r;
   Prof pr(DFLASH_PROF_ROWS, 1, (cudaStream_t)stream);
@@ -1162,6 +1176,7 @@ int dflash_embed_tokens_grad(const void* grad_out, int grad_dtype, const int32_t
     return fail(DFLASH_ERR_INVALID_ARG, "table_dtype must be DFLASH_DTYPE_BF16 or _F32");
   if (T > 0) {
     if (!token_ids) return fail(DFLASH_ERR_INVALID_ARG, "token_ids is null");
+    if ((r = check_words({{token_ids, "token_ids"}}))) return r;
     if ((r = check_ptr16(grad_out, "grad_out", grad_dtype))) return r;
   }
   if ((r = check_ptr16(grad_table, "grad_table", table_dtype))) return r;
@@ -1196,7 +1211,10 @@ int dflash_sample_tokens(const void* logits, int logits_dtype, int64_t row_strid
     return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
   int r;
   if ((r = check_elem_aligned(logits, "logits", logits_dtype))) return r;
-  if ((r = check_elem_aligned(probs, "probs", DFLASH_DTYPE_F32))) return r;
+  if ((r = check_words({{temperature, "temperature"}, {top_k, "top_k"}, {top_p, "top_p"},
+                        {min_p, "min_p"}, {uniforms, "uniforms"}, {tokens, "tokens"},
+                        {probs, "probs"}})))
+    return r;
   (void)ws;
   (void)ws_bytes;
   SamplingSettings s;
@@ -1238,6 +1256,11 @@ int dflash_verify_sampling_filtered(const void* logits, int logits_dtype,
     return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
   int r;
   if ((r = check_elem_aligned(logits, "logits", logits_dtype))) return r;
+  if ((r = check_words({{temperature, "temperature"}, {top_k, "top_k"}, {top_p, "top_p"},
+                        {min_p, "min_p"}, {draft_probs, "draft_probs"}, {draft, "draft"},
+                        {uniforms, "uniforms"}, {emitted, "emitted"},
+                        {num_emitted, "num_emitted"}, {accepted, "accepted"}})))
+    return r;
   if ((r = check_ws(ws, ws_bytes, filtered_verify_ws_bytes(B, gamma)))) return r;
   SamplingSettings s;
   s.temperature = temperature;

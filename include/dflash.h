@@ -403,7 +403,8 @@ DFLASH_API size_t dflash_sample_tokens_workspace_size(int R, int V); /* 0 */
  * Probabilities are within 2^-17 of their value.
  * A setting or uniform outside its range (or NaN) sets DFLASH_ERR_DEVICE_CHECK; its rows
  * give -1 and zeros.  R = 0 does nothing.
- * Errors: INVALID_ARG for sizes and null pointers; UNSUPPORTED for V > 2^19 or R > 2^24. */
+ * Errors: INVALID_ARG for sizes, null pointers and pointers that are not aligned to their
+ * element size; UNSUPPORTED for V > 2^19 or R > 2^24. */
 DFLASH_API int dflash_sample_tokens(const void* logits, int logits_dtype, int64_t row_stride,
                                     int R, int V, const float* temperature,
                                     const int32_t* top_k, const float* top_p,
@@ -426,7 +427,8 @@ DFLASH_API size_t dflash_verify_sampling_filtered_workspace_size(int B, int gamm
  * Outputs as dflash_verify_sampling.  A row that keeps no token (every logit -inf or NaN, or
  * a setting or uniform out of range, which also sets DFLASH_ERR_DEVICE_CHECK) rejects its
  * proposal and ends the block without a sample (num_emitted = accepted).
- * Errors: as dflash_verify_sampling; UNSUPPORTED for V > 2^19 or B * (gamma + 1) > 2^24. */
+ * Errors: as dflash_verify_sampling, and INVALID_ARG for pointers that are not aligned to their
+ * element size; UNSUPPORTED for V > 2^19 or B * (gamma + 1) > 2^24. */
 DFLASH_API int dflash_verify_sampling_filtered(
     const void* logits, int logits_dtype, const float* temperature, const int32_t* top_k,
     const float* top_p, const float* min_p, const float* draft_probs, const int32_t* draft,

@@ -98,3 +98,15 @@ def test_binding_refuses_other_tensors(cpu_lib):
         dflash.dflash_embed_tokens(x, t.long(), x)
     with pytest.raises(ValueError):
         dflash.dflash_embed_tokens_grad(x.double(), t, x)
+
+
+@pytest.mark.parametrize("name,good,kws", [
+    ("dflash_sample_tokens", SAMPLE, ("t", "k", "p", "m", "u", "tok")),
+    ("dflash_verify_sampling_filtered", VERIFY, ("t", "k", "p", "m", "q", "draft", "u", "em", "ne",
+                                                 "ac")),
+    ("dflash_embed_tokens", EMBED, ("ids",)), ("dflash_embed_tokens_grad", GRAD, ("ids",))])
+def test_pointers_off_their_elements(cpu_lib, name, good, kws):
+    for kw in kws:
+        for off in (1, 2, 3):
+            assert _call(getattr(cpu_lib, name), good, **{kw: P + off}) == BAD, (kw, off)
+            assert b"aligned" in cpu_lib.dflash_last_error()
