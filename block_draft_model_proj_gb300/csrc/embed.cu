@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 4) grad_sum_kernel(const GradArgs a)
   const int tid = threadIdx.x;
   __shared__ int s_key[kMaxChunk + 2], s_slot[kMaxChunk];
   const int chunk = blockIdx.x / a.col_tiles, tile = blockIdx.x % a.col_tiles;
-  const int p0 = chunk * a.chunk, p1 = min(a.T, p0 + a.chunk), n = p1 - p0;
+  const int p0 = chunk * a.chunk, n = min(a.chunk, a.T - p0);
   for (int i = tid; i < n + 2; i += kThreads) {
     const int p = p0 - 1 + i;
     s_key[i] = p >= 0 && p < a.T ? a.key[p] : -1;
@@ -541,11 +541,11 @@ EmbedGradLayout embed_grad_layout(int V, int D, int T, int sms, void* ws) {
     return p;
   };
   l.chunk = chunk_len(T, D, sms);
-  l.chunks = (T + l.chunk - 1) / l.chunk;
+  l.chunks = (int)(((long)T + l.chunk - 1) / l.chunk);  // T up to 2^31 - 1
   l.key[0] = reinterpret_cast<int32_t*>(take((size_t)T * 4));
   l.slot[0] = reinterpret_cast<int32_t*>(take((size_t)T * 4));
   if (T > kRankMax) {
-    l.tiles = (T + kTile - 1) / kTile;
+    l.tiles = (int)(((long)T + kTile - 1) / kTile);
     l.key[1] = reinterpret_cast<int32_t*>(take((size_t)T * 4));
     l.slot[1] = reinterpret_cast<int32_t*>(take((size_t)T * 4));
     l.hist = reinterpret_cast<uint32_t*>(take((size_t)l.tiles * kDigits * 4));
@@ -571,9 +571,10 @@ cudaError_t launch_embed(const void* table, int dtype, int V, int D, const int32
   // 16 slots per row of threads, fewer while that leaves SMs without a CTA or two
   const int ny = kThreads / tx;
   int rows = 16 * ny;
-  while (rows > 1 && (long)((T + rows - 1) / rows) * cols < 2L * sms) rows /= 2;
+  auto ctas = [&]() { return ((long)T + rows - 1) / rows; };
+  while (rows > 1 && ctas() * cols < 2L * sms) rows /= 2;
   if (rows > kMaxRows) rows = kMaxRows;
-  const dim3 grid((unsigned)((T + rows - 1) / rows), (unsigned)cols);
+  const dim3 grid((unsigned)ctas(), (unsigned)cols);
   auto go = [&](auto kernel, auto* t) {
     using E = std::remove_const_t<std::remove_pointer_t<decltype(t)>>;
     return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, t, V, D, ids, T, scale,

@@ -315,3 +315,29 @@ def test_forward_of_long_walks(lib, T, V, D, kind, dtype):
         wrong = (out.double() - scale * rows).abs() > \
             (0.0 if scale == 1.0 else _half(dtype) + 2 * 2.0 ** -24) * (scale * rows).abs()
         assert not wrong.any(), wrong.any(1).nonzero()[:8, 0].tolist()
+
+
+def test_the_most_slots(lib):
+    """2^31 - 1 slots: the last chunk's, tile's and CTA's ends lie at the end of the int range."""
+    import torch
+    import block_draft_model_proj_gb300 as dflash
+    T, V = 2**31 - 1, 5
+    table = torch.arange(1, V + 1, device="cuda").to(torch.bfloat16).view(V, 1)
+    ids = torch.randint(0, V, (T,), dtype=torch.int32, device="cuda")
+    ids[-3:] = torch.tensor([4, -1, 2], dtype=torch.int32, device="cuda")
+    out = torch.full((T, 1), 9.0, dtype=torch.bfloat16, device="cuda")
+    dflash.dflash_embed_tokens(table, ids, out)
+    dflash.dflash_device_status()
+    assert out[-3:, 0].tolist() == [5.0, 0.0, 3.0]
+    for i in range(0, T, 1 << 28):
+        e = min(T, i + (1 << 28))
+        assert torch.equal(out[i:e, 0], (ids[i:e] + 1).to(torch.bfloat16))
+    at = torch.cat([torch.tensor([0, T - 3, T - 2, T - 1], device="cuda"),
+                    torch.randint(0, T, (1000,), device="cuda")]).unique()
+    out.zero_()
+    out[at] = 1.0
+    grad = torch.full((V, 1), math.nan, device="cuda")
+    dflash.dflash_embed_tokens_grad(out, ids, grad)
+    dflash.dflash_device_status()
+    hit = ids[at]
+    assert torch.equal(grad[:, 0], torch.bincount(hit[hit >= 0], minlength=V).float())

@@ -110,3 +110,10 @@ def test_pointers_off_their_elements(cpu_lib, name, good, kws):
         for off in (1, 2, 3):
             assert _call(getattr(cpu_lib, name), good, **{kw: P + off}) == BAD, (kw, off)
             assert b"aligned" in cpu_lib.dflash_last_error()
+
+
+@pytest.mark.parametrize("T", [(1 << 31) - 1, (1 << 31) - 200, (1 << 31) - 2048])
+def test_gradient_workspace_of_the_most_slots(cpu_lib, T):
+    """Two buffers of sorted tokens and of their slots, whatever the rounding up to chunks."""
+    n = cpu_lib.dflash_embed_tokens_grad_workspace_size(2, 1, T)
+    assert 16 * T <= n <= 32 * T
