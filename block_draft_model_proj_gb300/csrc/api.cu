@@ -1215,6 +1215,12 @@ int dflash_sample_tokens(const void* logits, int logits_dtype, int64_t row_strid
                         {min_p, "min_p"}, {uniforms, "uniforms"}, {tokens, "tokens"},
                         {probs, "probs"}})))
     return r;
+  // the kernels write a row's zeros before they are done with its logits, and rows of another
+  // stride or type lie over one another
+  const __int128 l0 = (__int128)(uintptr_t)logits, p0 = (__int128)(uintptr_t)probs;
+  const __int128 l1 = l0 + ((__int128)(R - 1) * row_stride + V) * (int)esize(logits_dtype);
+  if (probs && p0 < l1 && l0 < p0 + (__int128)R * V * 4)
+    return fail(DFLASH_ERR_INVALID_ARG, "probs must not overlap logits");
   (void)ws;
   (void)ws_bytes;
   SamplingSettings s;

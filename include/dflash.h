@@ -397,7 +397,8 @@ DFLASH_API size_t dflash_sample_tokens_workspace_size(int R, int V); /* 0 */
  *   uniforms     [R] float32 in [0, 1)
  * Outputs: tokens [R] int32, the lowest index whose inclusive sum of kept p in index order
  * exceeds u times their total; probs [R, V] float32 or NULL, the kept tokens' renormalised
- * probabilities, 0 elsewhere.  A row without a logit above -inf gives token -1 and zeros.
+ * probabilities, 0 elsewhere (they must not overlap logits: INVALID_ARG).  A row without a logit
+ * above -inf gives token -1 and zeros.
  * Masses are 64-bit integer sums of weights accurate to about 2^-30: the same on every call,
  * and a decision differs from exact arithmetic only within that distance of its border.
  * Probabilities are within 2^-17 of their value.

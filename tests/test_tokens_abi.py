@@ -117,3 +117,15 @@ def test_gradient_workspace_of_the_most_slots(cpu_lib, T):
     """Two buffers of sorted tokens and of their slots, whatever the rounding up to chunks."""
     n = cpu_lib.dflash_embed_tokens_grad_workspace_size(2, 1, T)
     assert 16 * T <= n <= 32 * T
+
+
+@pytest.mark.parametrize("dt,ld,probs", [
+    (F32, 100, P), (F32, 120, P), (BF16, 100, P), (F32, 100, P + 4), (F32, 100, P + 4 * 399),
+    (F32, 120, P + 4 * 459), (F32, 1 << 40, P + 4 * (3 << 40)), (F32, 100, P - 4 * 399),
+    (F32, (1 << 62) + 7, P + (1 << 20))])
+def test_probabilities_in_the_logits(cpu_lib, dt, ld, probs):
+    """[4, 100] rows: probabilities that would be written over logits still to be read."""
+    at = 1 << 30
+    kw = dict(logits=at, dt=dt, ld=ld, probs=probs - P + at)
+    assert _call(cpu_lib.dflash_sample_tokens, SAMPLE, **kw) == BAD
+    assert b"overlap" in cpu_lib.dflash_last_error()
