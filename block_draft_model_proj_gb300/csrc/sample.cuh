@@ -124,11 +124,14 @@ constexpr int kMaxC = 8;             // CTAs per row (portable cluster size)
 constexpr int kOneBits = 44;         // w = 1 is 2^44: sums of 2^19 tokens stay below 2^63
 constexpr float kMinTemp = 1e-6f, kMaxTemp = 1e6f;
 constexpr float kFastLogit = 1e30f;   // fast weights need |M| below this (no overflow in x)
-// Relative error of sums of fast weights: ex2.approx 2^-22, its correction's roundings
-// 3 * 2^-24, sums 9 * 2^-24, the rounding of l - M (fp32 logits) about 20 * 2^-24 at the
-// |x| <= 32 that hold the mass -- below 2^-19 in all.
+// Error of a sum of fast weights over any of a row's tokens, relative to the row's total, in
+// units of 2^-24: ex2.approx 4, its correction's rounding 1, the additions of a step 8, and the
+// rounding of l - M, |x| ln 2 for a weight 2^x.  By weight |x| is 14.3 on average at most: beside
+// M's own weight, n weights of 2^-y have the mean a with n 2^-y (y - a) = a, largest at
+// y = a + 1 / ln 2, and n = 2^19 gives 14.26 -- 9.9 units.  23 in all: below 2^-19.
 constexpr int kFastBits = 19;
-// ... and of sums of rough weights: 3 * 2^-24 |x| ln 2 more, |x| <= 32.
+// ... and of rough weights: the roundings of x and of chi, 9.9 units each, are left in: 4 + 3
+// additions + 3 * 9.9, below 2^-18.
 constexpr int kRoughBits = 17;
 
 // round(2^(31 + j/32))

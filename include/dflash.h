@@ -378,7 +378,7 @@ DFLASH_API int dflash_verify_sampling(const void* logits, int logits_dtype, doub
 /* ---- 4c. filtered sampling and verification ([P3] Sampling with temperature is not argmax
  *      matching: the proposal distribution after top-k, temperature or a selector) -------- */
 
-DFLASH_API size_t dflash_sample_tokens_workspace_size(int R, int V); /* 0 */
+DFLASH_API size_t dflash_sample_tokens_workspace_size(int R, int V); /* 0: ws is not used */
 
 /* Draws one token from each of R rows of logits: a request's draft proposals, with the
  * distribution they were drawn from (the draft_probs of the verification calls).
@@ -386,7 +386,8 @@ DFLASH_API size_t dflash_sample_tokens_workspace_size(int R, int V); /* 0 */
  *                elements from one row to the next; -inf = a token that is never drawn; NaN
  *                counts as -inf; +inf entries share the whole probability equally
  *   temperature  [R / rows_per_request] float32 or NULL (1): p = softmax(logits / temperature);
- *                0 = greedy (the largest logit, lowest index); else in [1e-6, 1e6]
+ *                0 = greedy (the largest logit, lowest index); else in [1e-6, 1e6], where the
+ *                fp32 exponents stay finite for every pair of logits below 1e30
  *   min_p        the same shape or NULL: keeps the tokens with p_v >= min_p * max p; 0 = off
  *   top_k        int32, the same shape or NULL: then keeps the k largest logits (lowest index
  *                first on ties); 0 = off
@@ -399,9 +400,11 @@ DFLASH_API size_t dflash_sample_tokens_workspace_size(int R, int V); /* 0 */
  * exceeds u times their total; probs [R, V] float32 or NULL, the kept tokens' renormalised
  * probabilities, 0 elsewhere (they must not overlap logits: INVALID_ARG).  A row without a logit
  * above -inf gives token -1 and zeros.
- * Masses are 64-bit integer sums of weights accurate to about 2^-30: the same on every call,
- * and a decision differs from exact arithmetic only within that distance of its border.
- * Probabilities are within 2^-17 of their value.
+ * Masses are 64-bit integer sums of weights accurate to about 2^-30 of their value and 2^-45 of
+ * the largest weight: the same on every call, and a decision differs from exact arithmetic only
+ * where the masses it compares lie within 2^-30 of the row's total + V * 2^-45 of the largest
+ * weight.  Probabilities are within 2^-17 of their value (tokens below 2^-126 of the largest may
+ * come out as 0); they are written from faster weights than the token is drawn by.
  * A setting or uniform outside its range (or NaN) sets DFLASH_ERR_DEVICE_CHECK; its rows
  * give -1 and zeros.  R = 0 does nothing.
  * Errors: INVALID_ARG for sizes, null pointers and pointers that are not aligned to their
