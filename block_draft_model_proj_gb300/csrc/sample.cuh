@@ -40,17 +40,32 @@
 // cut by a radix selection on the logit's bits and then by index when it is large (long ties,
 // tokens beyond 2^-64 of the maximum).
 //
-// Measured (GB300, 151936 bf16 logits a row, device us of a call; "with q": probabilities
-// written too; the floor of 960 rows is 43 / 129 us):
-//   rows                  1      15     120    960    960 with q
-//   greedy                5.8    6.6    9.4    56     159
-//   top-k 50              11.8   13     17     102    206
-//   top-p 0.9, narrow     13     14     21     123    223
-//   unfiltered            11     14     27     142    291
-//   top-p 0.9, broad      39     47     92     532    808     (tens of thousands kept)
+// Measured (GB300, 151936 logits a row, temperature 0.85, device us of a call; "with q":
+// probabilities written too; the floor of 960 rows is 43 / 129 us in bf16, 86 / 172 in fp32).
+// Rows: N(0, 1.5) and 200 tokens falling off from 18 by 2 ln(rank), "broad" from 9 by ln(rank);
+// up to 120 rows are found in L2.
+//   bf16 rows             1      15     120    960    960 with q
+//   greedy                5.4    6.2    9.8    57     154
+//   min-p 0.05            10     11     16     94     196
+//   top-k 50              12     13     18     104    206
+//   top-p 0.9             13     14     22     131    225
+//   unfiltered            11     15     28     162    286
+//   min-p 0.001, broad    25     35     79     283    397
+//   top-k 400             27     29     70     293    487    (a list that is sorted)
+//   top-k 600 or 5000     30     35     83     458    615    (by value)
+//   top-p 0.9, broad      41     45     96     551    824    (tens of thousands kept)
+//   fp32 rows
+//   greedy                5.6    6.6    18     94     192
+//   top-k 50              11     12     28     190    310
+//   top-p 0.9             13     14     33     287    376
+//   unfiltered            12     14     41     259    412
+//   top-k 600 or 5000     27     31     94     584    706    (exact)
+//   min-p 0.001, broad    26     32     87     335    439
+//   top-p 0.9, broad      85     99     243    1247   1479   (exact)
 // Few rows are bound by dependent phases of about 1 us (cluster barriers, the gather, the
-// list), many rows by issue: the second pass, the weights, the list; broad nuclei by one
-// shared-memory atomic per token (about 8 cycles a warp) and by the look-up of the draw.
+// list).  Many rows that keep few tokens wait for loads in both passes and at barriers (issue
+// slots 31 to 41 % used); broad nuclei are bound by issue (64 %) with one shared-memory atomic
+// per token, fp32 ones by four of them and an exact weight per token.
 //
 // This header holds what a row's CTAs do; sample_*.cu compile filter_kernel for one type and
 // purpose each (side by side: the kernel is long), sample.cu holds the rest of the two calls.
