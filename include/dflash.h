@@ -431,6 +431,7 @@ DFLASH_API size_t dflash_verify_sampling_filtered_workspace_size(int B, int gamm
  * Outputs as dflash_verify_sampling.  A row that keeps no token (every logit -inf or NaN, or
  * a setting or uniform out of range, which also sets DFLASH_ERR_DEVICE_CHECK) rejects its
  * proposal and ends the block without a sample (num_emitted = accepted).
+ * The outputs must not overlap the inputs: requests are finished side by side.
  * Errors: as dflash_verify_sampling, and INVALID_ARG for pointers that are not aligned to their
  * element size; UNSUPPORTED for V > 2^19 or B * (gamma + 1) > 2^24. */
 DFLASH_API int dflash_verify_sampling_filtered(
